@@ -588,12 +588,13 @@ int ring_attn_block_norm_fwd(const void* x, const void* a, const float* post_w, 
  * h), with the forward's y, a and stats:
  *   dx = dy + N_pre'(dh),  da = N_post'(scale g dx)     as x, a
  *   dgate   [gate_rows][D], contiguous: fp32 sums over the rows of a gate row
- *           where gate_rows < M, else dtype_gate
+ *           where gate_rows < M or M == 0, else (a gate row a row) dtype_gate
  *   dpost_w, dpost_b, dpre_w, dpre_b   fp32 [D], overwritten: required for a
  *           weight that is given, optional otherwise (NULL: not wanted)
  * dx may be dy, da may be dh.  row_strides: dy, dh, y, a, gate, dx, da.
  * workspace: device, 256-byte aligned, of the size below; its contents on
- * entry do not matter.  M == 0 writes zero sums.
+ * entry do not matter.  M == 0 writes zero sums: the weights' gradients and
+ * all gate_rows rows of dgate (fp32), of those that are given.
  */
 size_t ring_attn_block_norm_bwd_workspace_size(long long M, int D, long long gate_rows, int flags);
 

@@ -413,11 +413,17 @@ int ring_attn_block_norm_bwd(const void* dy, const void* dh, const void* y, cons
     int rc = check_norm(M, D, gate_rows, dtype_x, dtype_a, dtype_gate, flags, scale);
     if (rc != RING_ATTN_OK) return rc;
     float* sums[] = {dpost_w, dpost_b, dpre_w, dpre_b};
-    if (M == 0) {  // sums over no rows
+    if (M == 0) {  // sums over no rows, the shared gate's fp32 ones among them
+      if (gate_rows > (1LL << 40)) return static_cast<int>(RING_ATTN_ERR_UNSUPPORTED);
+      auto clear = [&](void* s, long long rows) {
+        return !s || rows == 0 || cudaMemsetAsync(s, 0, static_cast<size_t>(rows) * D * 4, stream) == cudaSuccess;
+      };
+      for (void* s : {static_cast<void*>(dpost_w), static_cast<void*>(dpost_b), static_cast<void*>(dpre_w),
+                      static_cast<void*>(dpre_b), dgate})
+        if (!aligned_to(s, 4)) return static_cast<int>(RING_ATTN_ERR_UNSUPPORTED);
       for (float* s : sums)
-        if (s && cudaMemsetAsync(s, 0, static_cast<size_t>(D) * 4, stream) != cudaSuccess)
-          return static_cast<int>(RING_ATTN_ERR_CUDA);
-      return static_cast<int>(RING_ATTN_OK);
+        if (!clear(s, 1)) return static_cast<int>(RING_ATTN_ERR_CUDA);
+      return static_cast<int>(clear(dgate, gate_rows) ? RING_ATTN_OK : RING_ATTN_ERR_CUDA);
     }
     const bool post = flags & kNormPost, pre = flags & kNormPre, layer = flags & kNormLayer;
     const bool shared = gate_rows > 0 && gate_rows < M;

@@ -458,8 +458,9 @@ def ring_attn_block_norm_bwd(dy, dh, y, a, stats, post_weight=None, post_bias=No
     without a), a and stats, returns (dx, da, dgate, dpost_weight, dpost_bias,
     dpre_weight, dpre_bias), None for what the forward did not take.  dx, da
     are of y's and a's type, weights' gradients fp32; dgate [G, D] is fp32
-    where rows share a gate row, else of the gate's type and shape.  dx may be
-    dy, da may be dh."""
+    where rows share a gate row (zeros where there are no rows), else -- as
+    many gate rows as rows, one and one too -- of the gate's type and shape.
+    dx may be dy, da may be dh."""
     if torch is None:
         _lazy()
     x = y if y is not None else dy
@@ -511,7 +512,7 @@ def ring_attn_block_norm_bwd(dy, dh, y, a, stats, post_weight=None, post_bias=No
         elif a is not None:
             da = torch.empty(shape, dtype=block, device=dev)
         if gate is not None:
-            if G < M:
+            if G < M or M == 0 and G > 0:   # (no rows: sums over none, written as zeros)
                 dgate = torch.empty((G, D), dtype=torch.float32, device=dev)
             else:
                 dgate = torch.empty(gate.shape, dtype=gate.dtype, device=dev)

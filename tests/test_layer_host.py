@@ -312,6 +312,17 @@ def test_block_norm_bwd_refusals(lib):
     assert call(ws=at(3)) == capi.ERR_UNSUPPORTED    # ... over an input
 
 
+def test_block_norm_bwd_of_no_rows_refuses_what_it_cannot_clear(lib):
+    def call(**kw):
+        return norm_bwd_call(lib, **{**dict(M=0, ws=NUL, dy=NUL, dh=NUL, y=NUL, a=NUL, stats=NUL, dx=NUL, da=NUL), **kw})
+
+    assert call(G=(1 << 40) + 1) == capi.ERR_UNSUPPORTED
+    assert call(dg=at(11) + 2) == capi.ERR_UNSUPPORTED   # fp32 sums, whatever the gate's type
+    assert call(dg=at(11) + 2, tg=0) == capi.ERR_UNSUPPORTED
+    assert call(dw1=at(12) + 2) == capi.ERR_UNSUPPORTED
+    assert call(gate=NUL, G=0, dg=NUL, dw1=NUL, dw2=NUL) == capi.OK   # nothing to clear
+
+
 def test_block_norm_workspace_is_bounded_and_covers_shared_gates(lib):
     f = lib.ring_attn_block_norm_bwd_workspace_size
     small, large = f(4, 256, 0, POST | PRE), f(1 << 22, 256, 0, POST | PRE)
