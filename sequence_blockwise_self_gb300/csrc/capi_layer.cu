@@ -252,7 +252,7 @@ int check_grads(const void* const* grads, void* const* outs, const long long* n,
   // Each output, the norm and the workspace apart from one another and from
   // every gradient but an output's own, which it may be (same memory, same
   // type).
-  std::vector<Range> w(own, own + n_own);
+  std::vector<Range> w;
   w.reserve(2 * static_cast<size_t>(n_tensors) + n_own);
   for (int i = 0; i < n_tensors; ++i) {
     const GradTensor& g = (*list)[i];
@@ -262,7 +262,10 @@ int check_grads(const void* const* grads, void* const* outs, const long long* n,
     if (outs && g.in == g.out && g.dt_in == g.dt_out) continue;
     w.push_back({in, in + g.n * dtype_bytes(g.dt_in), false});
   }
-  std::sort(w.begin(), w.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  // (views of one buffer come in order: then a pass over them is enough)
+  auto below = [](const Range& a, const Range& b) { return a.lo < b.lo; };
+  if (!std::is_sorted(w.begin(), w.end(), below)) std::sort(w.begin(), w.end(), below);
+  for (int i = 0; i < n_own; ++i) w.insert(std::upper_bound(w.begin(), w.end(), own[i], below), own[i]);
   // in rising order: the ends reached so far by outputs and by gradients
   uintptr_t out_end = 0, in_end = 0;
   for (const Range& r : w) {

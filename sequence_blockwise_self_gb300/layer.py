@@ -535,9 +535,15 @@ def ring_attn_block_norm_bwd(dy, dh, y, a, stats, post_weight=None, post_bias=No
 class GradList:
     """A list of gradient tensors checked once, for the calls below every
     step: grads (None entries are left out) and, where the results go
-    elsewhere than in place, outs of the same sizes.  The tensors are kept and
-    their addresses taken anew at every call; their sizes, types and strides
-    must not change."""
+    elsewhere than in place, outs of the same sizes.  The tensors themselves
+    are kept: where every step makes new ones (zero_grad(set_to_none=True))
+    pass the sequence, not a kept list.  Each call takes the addresses anew; a
+    tensor found elsewhere than at the last call has had its storage replaced
+    and is checked again, and refused where its size, type, device or strides
+    are no longer what they were.  (The list holds the storages that it
+    checked, so an address that is the same is the same memory; one that a
+    tensor has left is free at the next call.)  A kept tensor must not be
+    resized or viewed otherwise over the storage that it has."""
 
     def __init__(self, grads, outs=None):
         if torch is None:
@@ -563,16 +569,38 @@ class GradList:
         self._dt_out = (ctypes.c_int * n)(*[_code(o.dtype, f"output {i}") for i, o in enumerate(self.outs)])
         self._pointers = ctypes.c_void_p * n
         self._workspace = int(load().ring_attn_grad_workspace_size(n))
+        self._tensors = tuple(self.grads if self.in_place else self.grads + self.outs)
+        self._types = [t.dtype for t in self._tensors]
+        self._seen, self._held = self._places(), self._storages()
 
     def __len__(self):
-        return len(self.grads)
+        return len(self._n)
+
+    def _places(self):
+        return array.array("Q", map(torch.Tensor.data_ptr, self._tensors))
+
+    def _storages(self):
+        return list(map(torch.Tensor.untyped_storage, self._tensors))
 
     def _addresses(self):
-        if not self.grads:
+        if not self._tensors:
             return None, None
-        take = torch.Tensor.data_ptr
-        ins = self._pointers.from_buffer(array.array("Q", map(take, self.grads)))
-        return ins, ins if self.in_place else self._pointers.from_buffer(array.array("Q", map(take, self.outs)))
+        at = self._places()
+        if at != self._seen:
+            self._check_again()
+            self._seen, self._held = at, self._storages()
+        ins = self._pointers.from_buffer(at)
+        return ins, ins if self.in_place else self._pointers.from_buffer(at, 8 * len(self))
+
+    def _check_again(self):
+        n = len(self)
+        for i, (t, dtype) in enumerate(zip(self._tensors, self._types)):
+            name = f"{'gradient' if i < n else 'output'} {i % n}"
+            _check(t, name, dtype, self.index)
+            if t.numel() != self._n[i % n]:
+                raise ValueError(f"{name} has {t.numel()} elements, {self._n[i % n]} when the list was made")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
 
 
 def _grads(grads, outs):
@@ -611,7 +639,7 @@ def ring_attn_grad_norm(grads, norm=None, workspace=None, stream=None):
     with allocating:
         norm = _norm_out(norm, g.index)
         ws, size = _grad_workspace(workspace, g._workspace, g.index)
-    _call(g.index, load().ring_attn_grad_norm, g._addresses()[0], g._n, g._dt, len(g.grads), norm.data_ptr(), ws.data_ptr(),
+    _call(g.index, load().ring_attn_grad_norm, g._addresses()[0], g._n, g._dt, len(g), norm.data_ptr(), ws.data_ptr(),
           size, raw)
     return norm
 
@@ -627,9 +655,9 @@ def ring_attn_grad_scale(grads, max_norm: float, norm, outs=None, stream=None):
     g = _grads(grads, outs)
     raw, _ = _stream(stream, g.index)
     ins, to = g._addresses()
-    _call(g.index, load().ring_attn_grad_scale, ins, to, g._n, g._dt, g._dt_out, len(g.grads), max_norm,
+    _call(g.index, load().ring_attn_grad_scale, ins, to, g._n, g._dt, g._dt_out, len(g), max_norm,
           _norm_out(norm, g.index).data_ptr(), raw)
-    return g.outs
+    return list(g.outs)
 
 
 def ring_attn_grad_clip(grads, max_norm: float, outs=None, norm=None, workspace=None, stream=None):
@@ -643,6 +671,6 @@ def ring_attn_grad_clip(grads, max_norm: float, outs=None, norm=None, workspace=
         norm = _norm_out(norm, g.index)
         ws, size = _grad_workspace(workspace, g._workspace, g.index)
     ins, to = g._addresses()
-    _call(g.index, load().ring_attn_grad_clip, ins, to, g._n, g._dt, g._dt_out, len(g.grads), max_norm, norm.data_ptr(),
+    _call(g.index, load().ring_attn_grad_clip, ins, to, g._n, g._dt, g._dt_out, len(g), max_norm, norm.data_ptr(),
           ws.data_ptr(), size, raw)
     return norm

@@ -214,3 +214,20 @@ def test_past_two_to_the_31_elements():
     assert float(norm) == 85.0
     assert g[-3:].tolist() == [torch.tensor(v * 0.2).to(BF).item() for v in (3.0, 4.0, 12.0)]
     assert g[0].item() == torch.tensor(84 * 0.2).to(BF).item() and not g[1:-3].any()
+
+
+def test_a_kept_list_refuses_a_tensor_that_became_another():
+    """Before anything is launched; where the tensor is as it was again, the
+    list is good again."""
+    g, h = rand(1000), rand(2000, dtype=BF, seed=1)
+    kept = ra.GradList([g, h])
+    whole = g.data
+    for new in (rand(10), whole.cpu(), whole.to(BF), rand(1).expand(1000), rand(1000, 2)[:, 0]):
+        g.data = new
+        for call in (ra.ring_attn_grad_norm, lambda k: ra.ring_attn_grad_clip(k, 0.05),
+                     lambda k: ra.ring_attn_grad_scale(k, 0.05, torch.ones((), device="cuda"))):
+            with pytest.raises((ValueError, TypeError)):
+                call(kept)
+    g.data = whole
+    before = [g.clone(), h.clone()]
+    check(None, [g, h], 0.05, ra.ring_attn_grad_clip(kept, 0.05), before)

@@ -1,7 +1,8 @@
 """What the layer operators' wrappers (layer.py) pass to the library, and what
 they refuse, without a GPU: host tensors stand in for device ones, and a
 recorder for the library."""
-import ctypes
+import gc
+import weakref
 
 import pytest
 import torch
@@ -62,3 +63,87 @@ def test_the_gradient_of_a_gate_per_token_over_no_rows(lib):
     x = torch.zeros(0, 16, dtype=BF)
     got = ra.ring_attn_block_norm_bwd(x, x, x, x, torch.zeros(2, 0), gate=x.clone())
     assert got[2].dtype == BF and got[2].shape == (0, 16)
+
+
+# -------------------------------------------------------------- gradient lists
+
+def clip(grads, **kw):
+    return ra.ring_attn_grad_clip(grads, 1.0, norm=torch.zeros(()), workspace=torch.empty(1 << 16, dtype=torch.uint8), **kw)
+
+
+def replaced_by(t, new):
+    t.data = new
+
+
+CHANGES = {
+    "a smaller storage": lambda t: replaced_by(t, torch.ones(5)),
+    "a larger storage": lambda t: replaced_by(t, torch.ones(500)),
+    "another type": lambda t: replaced_by(t, t.data.to(BF)),
+    "another type of the same bytes": lambda t: replaced_by(t, torch.ones(128, dtype=BF)),
+    "strided": lambda t: replaced_by(t, torch.ones(128)[::2]),
+    "one element for all": lambda t: replaced_by(t, torch.ones(1).expand(64)),
+}
+
+
+@pytest.mark.parametrize("change", CHANGES.values(), ids=CHANGES.keys())
+@pytest.mark.parametrize("which", ["gradient", "output"])
+def test_a_kept_list_refuses_a_tensor_that_became_another(lib, change, which):
+    """The counts and types that the list has would reach past the end of
+    another storage."""
+    grads, outs = [torch.ones(7), torch.ones(64), torch.ones(8, 3)], [torch.ones(7), torch.ones(64), torch.ones(24)]
+    kept = ra.GradList(grads, outs)
+    for call in (clip, lambda g: ra.ring_attn_grad_norm(g, norm=torch.zeros(()), workspace=torch.empty(1 << 16)),
+                 lambda g: ra.ring_attn_grad_scale(g, 1.0, torch.zeros(()))):
+        call(kept)
+    change((grads if which == "gradient" else outs)[1])
+    before = len(lib.calls)
+    for call in (clip, lambda g: ra.ring_attn_grad_norm(g, norm=torch.zeros(()), workspace=torch.empty(1 << 16)),
+                 lambda g: ra.ring_attn_grad_scale(g, 1.0, torch.zeros(()))):
+        for _ in range(2):   # refused again, not only once
+            with pytest.raises((ValueError, TypeError)):
+                call(kept)
+    assert len(lib.calls) == before
+
+
+def test_a_kept_list_passes_what_is_there_now(lib):
+    grads = [torch.ones(7), None, torch.ones(64), torch.empty(0)]
+    kept = ra.GradList(grads)
+    for _ in range(3):
+        clip(kept)
+        ins, outs, n, dt, dt_out, count = lib.last("ring_attn_grad_clip")[:6]
+        assert count == 3 and list(n) == [7, 64, 0] and list(dt) == list(dt_out) == [2, 2, 2]
+        assert [p or 0 for p in ins] == [p or 0 for p in outs] == [t.data_ptr() for t in grads if t is not None]
+        grads[2].data = torch.ones(64)   # as large: followed
+    outs = [torch.ones(7, dtype=BF), torch.ones(64)]
+    kept = ra.GradList([grads[0], grads[2]], outs)
+    clip(kept)
+    ins, to, n, dt, dt_out, count = lib.last("ring_attn_grad_clip")[:6]
+    assert list(ins) == [grads[0].data_ptr(), grads[2].data_ptr()] and list(to) == [t.data_ptr() for t in outs]
+    assert list(dt) == [2, 2] and list(dt_out) == [0, 2]
+
+
+def test_a_kept_list_is_not_changed_through_what_it_returns(lib):
+    grads = [torch.ones(7), torch.ones(64)]
+    kept = ra.GradList(grads)
+    for taken in (ra.ring_attn_grad_scale(kept, 1.0, torch.zeros(())), kept.grads, kept.outs, grads):
+        taken.append(torch.ones(3))
+        assert len(kept) == 2
+        clip(kept)
+        ins, _, n, _, _, count = lib.last("ring_attn_grad_clip")[:6]
+        assert count == 2 == len(n) == len(ins)
+
+
+def test_a_kept_list_holds_what_it_checked(lib):
+    """An address that a tensor has again is not another's memory: what was
+    checked there stays until the next call has found the tensor elsewhere."""
+    t = torch.ones(64)
+    kept = ra.GradList([t])
+    clip(kept)
+    first = weakref.ref(t.untyped_storage())
+    t.data = torch.ones(64)
+    gc.collect()
+    assert first() is not None
+    clip(kept)
+    gc.collect()
+    assert first() is None
+    assert list(lib.last("ring_attn_grad_clip")[0]) == [t.data_ptr()]
