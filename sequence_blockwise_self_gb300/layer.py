@@ -94,6 +94,13 @@ def _call(index, fn, *args):
         raise RingAttnError(rc, fn.__name__)
 
 
+def _workspace_bytes(workspace, index):
+    _check(workspace, "workspace", None, index)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -521,8 +528,7 @@ def ring_attn_block_norm_bwd(dy, dh, y, a, stats, post_weight=None, post_bias=No
             need = lib.ring_attn_block_norm_bwd_workspace_size(M, D, G, flags)
             workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
         else:
-            _check(workspace, "workspace", None, index)
-            need = workspace.numel() * workspace.element_size()
+            need = _workspace_bytes(workspace, index)
     _call(index, lib.ring_attn_block_norm_bwd, _p(dy), _p(dh) if pre else None, _p(y) if pre else None, _p(a),
           stats.data_ptr(), post_w, post_b, _p(gate), pre_w, dx.data_ptr(), _p(da), _p(dgate), _p(sums[0]), _p(sums[1]),
           _p(sums[2]), _p(sums[3]), _LL7(ld_dy, ld_dh, ld_y, ld_a, ld_g, ld_dx, ld_da), M, D, G, _code(dtype, "y"),
@@ -627,8 +633,7 @@ def grad_workspace_size(n_tensors: int) -> int:
 def _grad_workspace(workspace, need, index):
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index)), need
-    _check(workspace, "workspace", None, index)
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, _workspace_bytes(workspace, index)
 
 
 def ring_attn_grad_norm(grads, norm=None, workspace=None, stream=None):

@@ -147,3 +147,19 @@ def test_a_kept_list_holds_what_it_checked(lib):
     gc.collect()
     assert first() is None
     assert list(lib.last("ring_attn_grad_clip")[0]) == [t.data_ptr()]
+
+
+# ------------------------------------------------------------------- workspaces
+
+@pytest.mark.parametrize("workspace", [torch.empty(1, dtype=torch.uint8).expand(1 << 20), torch.empty(1 << 20)[::2],
+                                       torch.empty(1 << 10, 1 << 10).t()])
+def test_a_workspace_is_adjacent_memory(lib, workspace):
+    """An expanded tensor has fewer bytes than its shape says."""
+    x, st = torch.ones(4, 16, dtype=BF), torch.ones(2, 4)
+    with pytest.raises(ValueError):
+        ra.ring_attn_block_norm_bwd(x, x, x, x, st, workspace=workspace)
+    with pytest.raises(ValueError):
+        ra.ring_attn_grad_clip([torch.ones(7)], 1.0, norm=torch.zeros(()), workspace=workspace)
+    with pytest.raises(ValueError):
+        ra.ring_attn_grad_norm([torch.ones(7)], norm=torch.zeros(()), workspace=workspace)
+    assert all(n.endswith("workspace_size") for n, _ in lib.calls)
