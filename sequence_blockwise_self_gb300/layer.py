@@ -94,6 +94,13 @@ def _call(index, fn, *args):
         raise RingAttnError(rc, fn.__name__)
 
 
+def _int32(name, *sizes):
+    """Refuses sizes that the library's ints cannot hold (ctypes would cut
+    them)."""
+    if any(n >> 31 for n in sizes):
+        raise RingAttnError(capi.ERR_UNSUPPORTED, name)
+
+
 def _workspace_bytes(workspace, index):
     _check(workspace, "workspace", None, index)
     if not workspace.is_contiguous():
@@ -246,6 +253,12 @@ def _head_strides(t, name, shape, dtype, index):
     return s0, s1, s2
 
 
+def _position_map(*values):
+    if not all(-1 << 63 <= v < 1 << 63 for v in values):
+        raise ValueError(f"positions past 64 bits: {values}")
+    return _LL4(*values)
+
+
 def _rope(fn, names, ins, outs, rope, positions, interleaved, stream):
     if torch is None:
         _lazy()
@@ -261,6 +274,7 @@ def _rope(fn, names, ins, outs, rope, positions, interleaved, stream):
     if lead.dim() != 4:
         raise ValueError(f"{names[first]} must be [B, H, L, d]")
     B, _, L, d = lead.shape
+    _int32(fn.__name__, B, L, d, *[t.shape[1] for t in ins if t is not None and t.dim() == 4])
     raw, allocating = _stream(stream, index)
     strides = [0] * 18
     ptrs, heads, results = [None] * 6, [0, 0, 0], []
@@ -300,9 +314,9 @@ def _rope(fn, names, ins, outs, rope, positions, interleaved, stream):
     elif isinstance(positions, PositionMap):
         if positions.length != L:
             raise ValueError(f"the position map is of {positions.length} rows, the tensors have {L}")
-        pos_map = _LL4(*positions[1:])
+        pos_map = _position_map(*positions[1:])
     elif hasattr(positions, "__index__"):
-        pos_map = _LL4(L, positions.__index__(), 0, 1)
+        pos_map = _position_map(L, positions.__index__(), 0, 1)
     else:
         raise TypeError("positions must be None, an int, a PositionMap or a tensor")
     phase = rope.phase
@@ -416,6 +430,7 @@ def ring_attn_block_norm_fwd(x, a=None, post_weight=None, post_bias=None, gate=N
         raise ValueError("a gate, a post norm or y without a")
     if norm != "layer" and (post_bias is not None or pre_bias is not None):
         raise ValueError("a bias of a root-mean-square norm")
+    _int32("ring_attn_block_norm_fwd", D)
     M, dev = x.numel() // D, x.device
     raw, allocating = _stream(stream, index)
     flags = _norm_flags(norm, post and a is not None, pre, gate_sigmoid)
@@ -453,6 +468,7 @@ def _stats(stats, rows, M, index):
 
 
 def block_norm_bwd_workspace_size(M: int, D: int, gate_rows: int = 0, norm: str = "rms") -> int:
+    _int32("ring_attn_block_norm_bwd_workspace_size", int(D))
     return int(load().ring_attn_block_norm_bwd_workspace_size(int(M), int(D), int(gate_rows),
                                                               _norm_flags(norm, True, True, False)))
 
@@ -490,6 +506,7 @@ def ring_attn_block_norm_bwd(dy, dh, y, a, stats, post_weight=None, post_bias=No
         raise ValueError("pre-norm weights without the pre norm")
     if not post and (post_weight is not None or post_bias is not None):
         raise ValueError("post-norm weights without the post norm")
+    _int32("ring_attn_block_norm_bwd", D)
     M, dev = x.numel() // D, x.device
     raw, allocating = _stream(stream, index)
     flags = _norm_flags(norm, post and a is not None, pre, gate_sigmoid)

@@ -163,3 +163,53 @@ def test_a_workspace_is_adjacent_memory(lib, workspace):
     with pytest.raises(ValueError):
         ra.ring_attn_grad_norm([torch.ones(7)], norm=torch.zeros(()), workspace=workspace)
     assert all(n.endswith("workspace_size") for n, _ in lib.calls)
+
+
+# ------------------------------------------------- numbers that C types cannot hold
+
+FAR = (1 << 32) + 8   # 8 in 32 bits
+
+
+@pytest.mark.parametrize("shape", [(FAR, 1, 1, 4), (1, FAR, 1, 4), (1, 1, FAR, 4), (1, 1, 1, FAR)])
+def test_rotary_sizes_past_32_bits_are_refused(lib, shape):
+    """(Cut to 32 bits they would be 8, and the rest of the output never
+    written.)"""
+    q = torch.empty(shape, device="meta")
+    rope = ra.RotaryFrequencies(4, device="cpu")
+    for fn in (ra.ring_attn_rope_fwd, ra.ring_attn_rope_bwd):
+        for args, kw in (((q, None), dict(q_out=q)), ((None, q), dict(k_out=q)), ((None, None), dict(v=q, v_out=q))):
+            if fn is ra.ring_attn_rope_bwd:
+                kw = {"d" + k: v for k, v in kw.items()}
+            with pytest.raises(ra.RingAttnError):
+                fn(*args, rope, **kw)
+    assert not lib.calls
+
+
+def test_block_norm_columns_past_32_bits_are_refused(lib):
+    x, st = torch.empty(1, FAR, device="meta"), torch.ones(2, 1)
+    with pytest.raises(ra.RingAttnError):
+        ra.ring_attn_block_norm_fwd(x, None, h=x, stats=st)
+    with pytest.raises(ra.RingAttnError):
+        ra.ring_attn_block_norm_bwd(x, x, x, None, st, dx=x)
+    with pytest.raises(ra.RingAttnError):
+        ra.block_norm_bwd_workspace_size(1, FAR)
+    assert not lib.calls
+
+
+@pytest.mark.parametrize("positions", [1 << 63, -(1 << 63) - 1, (1 << 64) + 5, ra.PositionMap(4, 2, 1 << 63, 0, 1),
+                                       ra.PositionMap(4, 2, 0, 1 << 64, 1), ra.PositionMap(4, 2, 0, 0, 1 << 64),
+                                       ra.PositionMap(4, (1 << 64) + 2, 0, 0, 1)])
+def test_positions_past_64_bits_are_refused(lib, positions):
+    q = torch.zeros(1, 2, 4, 8)
+    with pytest.raises(ValueError):
+        ra.ring_attn_rope_fwd(q, None, ra.RotaryFrequencies(8, device="cpu"), positions)
+    assert not lib.calls
+
+
+def test_positions_of_64_bits_are_passed_on(lib):
+    q = torch.zeros(1, 2, 4, 8)
+    rope = ra.RotaryFrequencies(8, device="cpu")
+    for p, want in (((1 << 63) - 1, [4, (1 << 63) - 1, 0, 1]), (-(1 << 63), [4, -(1 << 63), 0, 1]),
+                    (ra.PositionMap(4, 2, -5, 1 << 62, -3), [2, -5, 1 << 62, -3])):
+        ra.ring_attn_rope_fwd(q, None, rope, p)
+        assert list(lib.last("ring_attn_rope_fwd")[-2]) == want
