@@ -156,11 +156,25 @@ __global__ void __launch_bounds__(kThreads, 4) grad_squares_kernel(const __grid_
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
-// o = c g: packs of V elements, 16 bytes of the wider type (a warp's accesses
+// out = g c d with d = 1, or where max / n is below 2^-100 c = 2^100 max / n
+// and d = 2^-100: a subnormal factor would have lost bits that the product
+// has.  (There max is below 2^28, n above 2^-49: nothing on the way leaves the
+// range, and c is at most 1.)
+struct Factor {
+  float c, d;
+  __device__ __forceinline__ float operator()(float g) const { return g * c * d; }
+};
+__device__ __forceinline__ Factor factor_of(float max_norm, float n) {
+  const float c = max_norm / n;
+  if (c >= 0x1p-100f) return {c, 1.f};
+  return {max_norm * 0x1p64f / (n * 0x1p-36f), 0x1p-100f};
+}
+
+// o = f(g): packs of V elements, 16 bytes of the wider type (a warp's accesses
 // to both are consecutive), from its first aligned one on, where the other
 // type's is aligned too; else by element.
 template <typename T, typename U>
-__device__ void scale_chunk(const T* g, U* o, int n, float c) {
+__device__ void scale_chunk(const T* g, U* o, int n, Factor f) {
   constexpr int V = 16 / (sizeof(T) > sizeof(U) ? sizeof(T) : sizeof(U));
   int head = sizeof(T) > sizeof(U) ? head_of(g, n) : head_of(o, n);
   if (reinterpret_cast<uintptr_t>(g + head) % (V * sizeof(T)) || reinterpret_cast<uintptr_t>(o + head) % (V * sizeof(U))) head = n;
@@ -174,7 +188,7 @@ __device__ void scale_chunk(const T* g, U* o, int n, float c) {
     Pack<U, V> q;
     *reinterpret_cast<In*>(&p) = w;
 #pragma unroll
-    for (int j = 0; j < V; ++j) q.e[j] = from_f32<U>(to_f32(p.e[j]) * c);
+    for (int j = 0; j < V; ++j) q.e[j] = from_f32<U>(f(to_f32(p.e[j])));
     return *reinterpret_cast<Out*>(&q);
   };
   // four loads before their stores (which might be to the same memory: the
@@ -190,15 +204,15 @@ __device__ void scale_chunk(const T* g, U* o, int n, float c) {
   for (; k < packs; k += kThreads) to[k] = scaled(from[k]);
   for (k = threadIdx.x; k < head + (n - tail); k += kThreads) {
     const int at = k < head ? k : tail + (k - head);
-    o[at] = from_f32<U>(to_f32(g[at]) * c);
+    o[at] = from_f32<U>(f(to_f32(g[at])));
   }
 }
 
 template <typename T>
-__device__ void scale_to(const T* g, void* out, int dt, int chunk, long long n, float c) {
+__device__ void scale_to(const T* g, void* out, int dt, int chunk, long long n, Factor f) {
   auto scale = [&](auto o) {
     const Span at = sizeof(*g) > sizeof(*o) ? span_of(g, chunk, n) : span_of(o, chunk, n);
-    scale_chunk(g + at.lo, o + at.lo, at.n, c);
+    scale_chunk(g + at.lo, o + at.lo, at.n, f);
   };
   switch (dt) {
     case kBf16: scale(static_cast<__nv_bfloat16*>(out)); break;
@@ -208,7 +222,7 @@ __device__ void scale_to(const T* g, void* out, int dt, int chunk, long long n, 
 }
 
 // partials > 0: the norm is their root sum, written to *norm by one CTA;
-// else it is read from *norm.  norm_only: no tensor is touched.
+// else it is read from *norm.
 template <int N>
 __global__ void __launch_bounds__(kThreads, 4) grad_scale_kernel(const __grid_constant__ Table<N> t, const double* partial,
                                                               int partials, float* norm, float max_norm, int write_norm) {
@@ -225,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 4) grad_scale_kernel(const __grid_co
   }
   // a norm that is not finite leaves the values as they are
   const bool clip = n > max_norm && n <= 3.402823466e38f;
-  const float c = clip ? max_norm / n : 1.f;
+  const Factor f = clip ? factor_of(max_norm, n) : Factor{1.f, 1.f};
   const int chunks = t.first[t.count];
   for (int i = blockIdx.x; i < chunks; i += gridDim.x) {
     const int j = chunks - 1 - i;
@@ -233,9 +247,9 @@ __global__ void __launch_bounds__(kThreads, 4) grad_scale_kernel(const __grid_co
     if (!clip && t.in[k] == t.out[k]) continue;
     const int dt = t.dt[k] >> 2, chunk = j - t.first[k];
     switch (t.dt[k] & 3) {
-      case kBf16: scale_to(static_cast<const __nv_bfloat16*>(t.in[k]), t.out[k], dt, chunk, t.n[k], c); break;
-      case kFp16: scale_to(static_cast<const __half*>(t.in[k]), t.out[k], dt, chunk, t.n[k], c); break;
-      default: scale_to(static_cast<const float*>(t.in[k]), t.out[k], dt, chunk, t.n[k], c); break;
+      case kBf16: scale_to(static_cast<const __nv_bfloat16*>(t.in[k]), t.out[k], dt, chunk, t.n[k], f); break;
+      case kFp16: scale_to(static_cast<const __half*>(t.in[k]), t.out[k], dt, chunk, t.n[k], f); break;
+      default: scale_to(static_cast<const float*>(t.in[k]), t.out[k], dt, chunk, t.n[k], f); break;
     }
   }
 }

@@ -231,3 +231,17 @@ def test_a_kept_list_refuses_a_tensor_that_became_another():
     g.data = whole
     before = [g.clone(), h.clone()]
     check(None, [g, h], 0.05, ra.ring_attn_grad_clip(kept, 0.05), before)
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("value,max_norm", [(5e37, 1.0), (1e37, 1e-3), (1e36, 1e-8), (3e37, 3e-30)])
+def test_a_factor_below_the_normal_range(value, max_norm, dtype):
+    """max_norm / norm is subnormal in fp32, the clipped values are not: they
+    keep their bits."""
+    grads = [torch.full((20,), value, dtype=dtype, device="cuda"), rand(100, seed=1, mul=value / 50).clamp(-value, value)]
+    grads[0][::3] *= -0.25
+    before = [g.clone() for g in grads]
+    norm = ra.ring_attn_grad_clip(grads, max_norm)
+    check(None, grads, max_norm, norm, before)
+    again = [g.clone() for g in before]
+    check(None, ra.ring_attn_grad_scale(again, max_norm, norm), max_norm, norm, before)
