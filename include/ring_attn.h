@@ -522,7 +522,8 @@ enum { RING_ATTN_DTYPE_BF16 = 0, RING_ATTN_DTYPE_FP16 = 1, RING_ATTN_DTYPE_FP32 
  *            strides.  Each output may be its input.
  *   phase    device uint64 [rotary_dim/2]: f_i as the fraction of a turn per
  *            position, round(2^64 f_i / (2 pi)) modulo 2^64.  pos * phase is
- *            an exact product modulo a turn: no position is too far.
+ *            an exact product modulo a turn; the phase's own rounding, 2^-65 of
+ *            a turn a position, stays below fp32's to positions of 2^40.
  *   factor   of cos and sin (1, or the attention factor of a scaled context)
  *   positions        device, positions_bytes 4 or 8 (int32, int64): token l of
  *                    batch b at [b * positions_batch + l]; any value, negative
@@ -615,10 +616,14 @@ int ring_attn_block_norm_bwd(const void* dy, const void* dh, const void* y, cons
  *                          other ranks have added to, for instance)
  *   ring_attn_grad_clip    both
  * outs[i] of out_dtypes[i] (out_dtypes NULL: as dtypes) may be grads[i] where
- * the types agree; a tensor twice, or overlapping ones, are refused.  norm:
- * device fp32.  The sum is right for every finite value (it is rescaled where
- * fp32 squares would leave their range).  A norm that is not finite leaves
- * the values as they are: the caller sees it in *norm.  max_norm >= 0.
+ * the types agree.  An output that overlaps another output, another tensor's
+ * gradient, the norm or the workspace is refused (one listed twice in place,
+ * for instance).  Gradients alone are only read: one listed twice counts
+ * twice in the norm, so that of tied weights is listed once.  norm: device
+ * fp32.  The sum is right for every finite value (it is rescaled where fp32
+ * squares would leave their range).  A norm that is not finite, because a
+ * value is not or because it is beyond fp32's range, leaves the values as they
+ * are: the caller sees it in *norm.  max_norm >= 0.
  * workspace: device, 256-byte aligned, of the size below.
  */
 size_t ring_attn_grad_workspace_size(int n_tensors);

@@ -23,7 +23,10 @@ namespace ra {
 namespace norm {
 
 constexpr int kLayerThreads = 384;  // where a layer norm's sums over rows fit the registers at 16 columns
-constexpr int kCtas = 152;  // one CTA an SM, one row of partial sums each
+// One CTA an SM of a GB300, one row of partial sums each: fixed, so that the
+// workspace and the order of the sums, and with it the bits, are the same on
+// any device.  (One with fewer SMs takes the CTAs in turns.)
+constexpr int kCtas = 152;
 
 // Columns and rows at a time.  16 columns a thread and one row a step keep
 // two groups of warps an SM apart at 3584 columns (32768 rows of a

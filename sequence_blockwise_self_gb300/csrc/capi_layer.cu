@@ -300,7 +300,6 @@ int grads_run(Clip what, const void* const* grads, void* const* outs, const long
   a.norm = norm;
   a.partial = static_cast<double*>(ws);
   std::lock_guard<std::mutex> lock(g_mutex);
-  if ((rc = sm_count(&a.n_sms)) != RING_ATTN_OK) return rc;
   Timed t(RING_ATTN_KERNEL_GRAD_CLIP, stream);
   const cudaError_t e = what == Clip::kNorm    ? launch_grad_norm(a, stream)
                         : what == Clip::kScale ? launch_grad_scale(a, stream)
@@ -489,7 +488,6 @@ int ring_attn_block_norm_bwd(const void* dy, const void* dh, const void* y, cons
     p.scale = scale;
     p.partial = static_cast<float*>(workspace);
     std::lock_guard<std::mutex> lock(g_mutex);
-    if ((rc = sm_count(&p.n_sms)) != RING_ATTN_OK) return rc;
     Timed t(RING_ATTN_KERNEL_BLOCK_NORM, stream);
     return static_cast<int>(launch_block_norm_bwd(p, stream) == cudaSuccess ? RING_ATTN_OK : RING_ATTN_ERR_CUDA);
   });

@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr long long kChunk = 16384;  // elements
-constexpr int kMaxCtas = 608;        // partial sums of one launch: four an SM, all resident
+constexpr int kMaxCtas = 608;  // partial sums of one launch: four an SM of a GB300, on any device (the sums' order)
 constexpr long long kKeptBytes = 80LL << 20;  // of the L2, between the launches
 
 // The tensors of one launch, in the kernel's parameters: no copy to the

@@ -55,7 +55,7 @@ struct BlockNormArgs {
   int D = 0, flags = 0, dt_x = 0, dt_a = 0, dt_gate = 0;
   float scale = 1.f, eps = 0.f;
   float* partial = nullptr;  // backward workspace
-  int n_sms = 0;
+  int n_sms = 0;             // (forward)
 };
 cudaError_t launch_block_norm_fwd(const BlockNormArgs& a, cudaStream_t stream);
 cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, cudaStream_t stream);
@@ -74,7 +74,6 @@ struct GradArgs {
   float max_norm = 0.f;
   float* norm = nullptr;
   double* partial = nullptr;  // workspace
-  int n_sms = 0;
 };
 size_t grad_workspace_bytes(int n_tensors);
 cudaError_t launch_grad_norm(const GradArgs& a, cudaStream_t stream);

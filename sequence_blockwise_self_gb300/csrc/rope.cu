@@ -9,7 +9,8 @@
 // 0.06), and 64-bit arithmetic is slow here, so the frequency is kept in
 // turns as a 64-bit fraction: pos * phase modulo 2^64 is an exact integer
 // product whose top 32 bits are the fraction of a turn, whatever the
-// position and its sign; sincospi of it is right to fp32.
+// position's sign; sincospi of it is right to fp32.  (The fraction's own
+// rounding, 2^-65 a position, stays below fp32's to positions of 2^40.)
 //
 // Bound by HBM: every element is read once and written once.  A thread's
 // angles serve up to 12 heads, so the sines cost 1/12 of a pair's loads, and

@@ -213,7 +213,7 @@ class RotaryFrequencies:
                 if not beta_fast > beta_slow > 0:
                     raise ValueError("needs beta_fast > beta_slow > 0")
 
-                def index(turns):  # the pair, as an element index, that turns so often over original_length
+                def index(turns):  # the pair (a fraction of one too) that turns so often over original_length
                     return R * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
 
                 low, high = max(math.floor(index(beta_fast)), 0), min(math.ceil(index(beta_slow)), R - 1)
@@ -655,7 +655,8 @@ def _grad_workspace(workspace, need, index):
 
 def ring_attn_grad_norm(grads, norm=None, workspace=None, stream=None):
     """sqrt of the sum of squares over all tensors of `grads` (a sequence, or
-    a GradList), as an fp32 tensor of one element on their device."""
+    a GradList), as an fp32 tensor of one element on their device.  A tensor
+    listed twice counts twice."""
     g = _grads(grads, None)
     raw, allocating = _stream(stream, g.index)
     with allocating:
@@ -686,7 +687,8 @@ def ring_attn_grad_clip(grads, max_norm: float, outs=None, norm=None, workspace=
     """Clips the tensors of `grads` (a sequence, or a GradList) to a global
     norm of max_norm: ring_attn_grad_norm and ring_attn_grad_scale in one
     call, in place unless `outs` is given.  Returns the norm before clipping
-    (an fp32 tensor of one element); the host does not wait for it."""
+    (an fp32 tensor of one element); the host does not wait for it.  Where it
+    is not finite the values stay as they are."""
     g = _grads(grads, outs)
     raw, allocating = _stream(stream, g.index)
     with allocating:
