@@ -94,10 +94,10 @@ def _call(index, fn, *args):
         raise RingAttnError(rc, fn.__name__)
 
 
-def _int32(name, *sizes):
-    """Refuses sizes that the library's ints cannot hold (ctypes would cut
-    them)."""
-    if any(n >> 31 for n in sizes):
+def _int32(name, size):
+    """Refuses a size (or several or'ed) that the library's ints cannot hold:
+    ctypes would cut it."""
+    if size >> 31:
         raise RingAttnError(capi.ERR_UNSUPPORTED, name)
 
 
@@ -274,7 +274,7 @@ def _rope(fn, names, ins, outs, rope, positions, interleaved, stream):
     if lead.dim() != 4:
         raise ValueError(f"{names[first]} must be [B, H, L, d]")
     B, _, L, d = lead.shape
-    _int32(fn.__name__, B, L, d, *[t.shape[1] for t in ins if t is not None and t.dim() == 4])
+    _int32(fn.__name__, B | L | d)
     raw, allocating = _stream(stream, index)
     strides = [0] * 18
     ptrs, heads, results = [None] * 6, [0, 0, 0], []
@@ -286,6 +286,7 @@ def _rope(fn, names, ins, outs, rope, positions, interleaved, stream):
                     raise ValueError(f"{names[i]}_out without {names[i]}")
                 continue
             H = t.shape[1] if t.dim() == 4 else 0
+            _int32(fn.__name__, H)
             shape = (B, H, L, d)
             strides[3 * i:3 * i + 3] = _head_strides(t, names[i], shape, dtype, index)
             if out is None:
