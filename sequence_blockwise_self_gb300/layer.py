@@ -570,6 +570,17 @@ class GradList:
     resized or viewed otherwise over the storage that it has."""
 
     def __init__(self, grads, outs=None):
+        self._take(grads, outs)
+        self._types = [t.dtype for t in self._tensors]
+        self._seen, self._held = self._places(), self._storages()
+
+    @classmethod
+    def _for_one_call(cls, grads, outs):
+        g = cls.__new__(cls)
+        g._take(grads, outs)
+        return g
+
+    def _take(self, grads, outs):
         if torch is None:
             _lazy()
         grads = list(grads)
@@ -594,8 +605,7 @@ class GradList:
         self._pointers = ctypes.c_void_p * n
         self._workspace = int(load().ring_attn_grad_workspace_size(n))
         self._tensors = tuple(self.grads if self.in_place else self.grads + self.outs)
-        self._types = [t.dtype for t in self._tensors]
-        self._seen, self._held = self._places(), self._storages()
+        self._held = None
 
     def __len__(self):
         return len(self._n)
@@ -610,7 +620,7 @@ class GradList:
         if not self._tensors:
             return None, None
         at = self._places()
-        if at != self._seen:
+        if self._held is not None and at != self._seen:
             self._check_again()
             self._seen, self._held = at, self._storages()
         ins = self._pointers.from_buffer(at)
@@ -632,7 +642,7 @@ def _grads(grads, outs):
         if outs is not None:
             raise ValueError("a GradList has its outputs already")
         return grads
-    return GradList(grads, outs)
+    return GradList._for_one_call(grads, outs)
 
 
 def _norm_out(norm, index):
