@@ -14,8 +14,9 @@
 //
 // Bound by HBM where the row sums let it: 32768 x 3584 in bf16 218 us, 0.96
 // of the copy rate; layer
-// norms, with twice the sums, 274 us (0.76), with a gate per token 20000 x
-// 4096 230 us (0.84); rows of 3583, whose accesses are shifted, half of it.
+// norms, with twice the sums, 283 us (0.74), with a gate per token 20000 x
+// 4096 219 us (0.88 with the gate's bytes); rows of 3583, whose accesses are
+// shifted and whose sums spill, 481 us (0.43) and 662 us (layer norms).
 #pragma once
 #include "block_norm.cuh"
 
@@ -33,8 +34,8 @@ constexpr int kCtas = 152;
 // root-mean-square norm: 228 us, against 255 us with eight columns and two
 // rows a step, one barrier for both).  A layer norm's four sums over rows do
 // not fit 128 registers that way, and what spills falls out of the L1 that
-// the ring leaves (32768 x 3584 359 us against 274 us, 20000 x 4096 with a
-// gate per token 388 us against 230 us); wider than 4096 columns 16 it is,
+// the ring leaves (32768 x 3584 382 us against 283 us, 20000 x 4096 with a
+// gate per token 354 us against 219 us); wider than 4096 columns 16 it is,
 // with 168 registers up to 6144.  And up to 256 columns half of each warp
 // would idle (65536 x 256: 52 us against 37 us).
 inline int packs_for(int D, bool vec, bool layer) {

@@ -8,7 +8,8 @@ namespace {
 // 16 columns a thread.  Measured at 131072 x 3584 in bf16: eight columns and
 // one group of 14 warps a CTA 731 us, that with two rows a step (one barrier
 // for both) 673 us, one row a step in two such CTAs an SM 615 us, 16 columns
-// in two groups 558 us: 0.99 of the copy rate.
+// in two groups 558 us: 0.99 of the copy rate.  (Over inputs that change from
+// call to call 574 us, 0.97.)
 constexpr int V = 2;
 constexpr int kMost = 768, kGroups = 12;  // threads and groups of several warps of a CTA
 constexpr size_t kAhead = 60 * 1024;      // bytes fetched ahead
@@ -221,7 +222,10 @@ cudaError_t launch_block_norm_fwd(const BlockNormArgs& a, cudaStream_t stream) {
   // ring is not, but is asked for by all groups that share it at once: kept
   // from one and a half rows of a group on (32768 x 3584, 456 groups, layer
   // norm: 256 rows of a gate row kept 268 us, from the ring 202 us, 1024 rows
-  // 219 and 203 us; 9993 x 1000, 1672 groups, 3331 rows: 32 and 42 us).
+  // 219 and 203 us; 9993 x 1000, 1672 groups, 3331 rows: 32 and 42 us).  The
+  // rows of a group alone do not part the two sides: 1024 rows, 2.2 of a group,
+  // are kept although the ring would be faster, for the sake of 3331 rows, 2.0
+  // of a group, where it is slower.
   if (a.gate && a.gate_rows > 1) {
     const long long rows = a.M / a.gate_rows, most = static_cast<long long>(a.n_sms) * (kMost / threads);
     gate_from = rows == 1 || (2 * rows < 3 * most && a.M <= 0xffffffffLL) ? kRing : kKept;

@@ -8,12 +8,12 @@
 // before the first write -- the second time back to front, where L2 still
 // holds what the first launch read last.
 //
-// Bound by HBM.  Measured: 103 M fp32 elements to bf16 157 us, 822 MB read and 206 MB written less what L2 keeps (of the first
-// reading's 411 MB about 42 MB): 0.92 of the copy rate (183 us before four
-// loads in flight and the back to front order); 401 bf16 tensors of 100 M
-// elements at odd offsets 103 us on the GPU (109 us with eight CTAs an SM and
-// every chunk's ends element by element), as long as the host takes for their
-// addresses.  Chunks of 4096 elements instead of 16384: 198 us.  Streaming
+// Bound by HBM.  Measured: 103 M fp32 elements to bf16 158 us, 822 MB read and
+// 206 MB written less what L2 keeps (of the first reading's 411 MB about 42
+// MB): 0.92 of the copy rate (183 us before four loads in flight and the back
+// to front order); 401 bf16 tensors of 100 M elements at odd offsets 102 us on
+// the GPU (109 us with eight CTAs an SM and every chunk's ends element by
+// element), as long as the host takes for their addresses.  Chunks of 4096 elements instead of 16384: 198 us.  Streaming
 // hints on the second launch's loads and stores: no gain.  A small clipping
 // takes 6 to 9 us in a graph, two launches; the second starts while the first
 // ends.
