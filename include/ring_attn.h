@@ -625,6 +625,7 @@ int ring_attn_block_norm_bwd(const void* dy, const void* dh, const void* y, cons
  * value is not or because it is beyond fp32's range, leaves the values as they
  * are: the caller sees it in *norm.  max_norm >= 0.
  * workspace: device, 256-byte aligned, of the size below.
+ * Supported: 2^40 elements a tensor, 2^44 in all.
  */
 size_t ring_attn_grad_workspace_size(int n_tensors);
 

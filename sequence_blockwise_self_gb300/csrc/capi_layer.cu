@@ -239,9 +239,11 @@ int check_grads(const void* const* grads, void* const* outs, const long long* n,
   if (n_tensors == 0) return RING_ATTN_OK;
   if (!grads || !n || !dt) return RING_ATTN_ERR_NULL;
   list->resize(n_tensors);
+  long long total = 0;  // (a launch counts its chunks in 32 bits)
   for (int i = 0; i < n_tensors; ++i) {
     if (n[i] < 0) return RING_ATTN_ERR_SHAPE;
     if (!dtype_ok(dt[i]) || (dt_out && !dtype_ok(dt_out[i])) || n[i] > (1LL << 40)) return RING_ATTN_ERR_UNSUPPORTED;
+    if ((total += n[i]) > (1LL << 44)) return RING_ATTN_ERR_UNSUPPORTED;
     GradTensor& g = (*list)[i];
     g = {grads[i], outs ? outs[i] : nullptr, n[i], dt[i], dt_out ? dt_out[i] : dt[i]};
     if (n[i] == 0) continue;

@@ -399,6 +399,16 @@ def test_grad_norm_and_scale_refusals(lib):
     assert lib.ring_attn_grad_scale(p, p, n, dt, None, 1, 1.0, at(1), NUL) == capi.ERR_UNSUPPORTED
 
 
+def test_grad_norm_refuses_more_elements_than_chunks_can_count(lib):
+    """The same gradient many times is no conflict; past 2^44 elements in all
+    the chunks of a launch would not be counted in 32 bits."""
+    def call(k):
+        return lib.ring_attn_grad_norm(grads_of([at(1)] * k), (LL * k)(*[1 << 40] * k), (ctypes.c_int * k)(*[0] * k), k,
+                                       at(1) + (1 << 60), at(1) + (1 << 61), lib.ring_attn_grad_workspace_size(k), NUL)
+
+    assert call(17) == call(1000) == capi.ERR_UNSUPPORTED
+
+
 # ------------------------------------------------------- the package's own checks
 
 def test_wrappers_refuse_host_tensors():
