@@ -13,10 +13,10 @@
 // MB): 0.92 of the copy rate (183 us before four loads in flight and the back
 // to front order); 401 bf16 tensors of 100 M elements at odd offsets 102 us on
 // the GPU (109 us with eight CTAs an SM and every chunk's ends element by
-// element), as long as the host takes for their addresses.  Chunks of 4096 elements instead of 16384: 198 us.  Streaming
-// hints on the second launch's loads and stores: no gain.  A small clipping
-// takes 6 to 9 us in a graph, two launches; the second starts while the first
-// ends.
+// element), as long as the host takes for their addresses.  Chunks of 4096
+// elements instead of 16384: 198 us.  Streaming hints on the second launch's
+// loads and stores: no gain.  A small clipping takes 6 to 9 us in a graph, two
+// launches; the second starts while the first ends.
 #include <algorithm>
 #include <type_traits>
 
@@ -158,15 +158,15 @@ __global__ void __launch_bounds__(kThreads, 4) grad_squares_kernel(const __grid_
 
 // out = g c d with d = 1, or where max / n is below 2^-100 c = 2^100 max / n
 // and d = 2^-100: a subnormal factor would have lost bits that the product
-// has.  (There max is below 2^28, n above 2^-49: nothing on the way leaves the
-// range, and c is at most 1.)
+// has.  (There max is below 2^28 and n above 2^-49, but for a max of 0:
+// nothing on the way leaves the range, and c is at most 1.)
 struct Factor {
   float c, d;
   __device__ __forceinline__ float operator()(float g) const { return g * c * d; }
 };
 __device__ __forceinline__ Factor factor_of(float max_norm, float n) {
   const float c = max_norm / n;
-  if (c >= 0x1p-100f) return {c, 1.f};
+  if (c >= 0x1p-100f || max_norm == 0.f) return {c, 1.f};
   return {max_norm * 0x1p64f / (n * 0x1p-36f), 0x1p-100f};
 }
 

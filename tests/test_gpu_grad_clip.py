@@ -245,3 +245,27 @@ def test_a_factor_below_the_normal_range(value, max_norm, dtype):
     check(None, grads, max_norm, norm, before)
     again = [g.clone() for g in before]
     check(None, ra.ring_attn_grad_scale(again, max_norm, norm), max_norm, norm, before)
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("value", [3e-39, 1e-36, 1e-30, 1.0, 1e37])
+def test_a_limit_of_zero(value, dtype):
+    """Zeros, however small the norm."""
+    grads = [torch.full((40,), value, dtype=dtype, device="cuda"), torch.zeros(10, device="cuda")]
+    ra.ring_attn_grad_clip(grads, 0.0)
+    assert all((g == 0).all() for g in grads)
+    out = torch.ones(40, device="cuda")
+    ra.ring_attn_grad_scale([torch.full((40,), value, dtype=dtype, device="cuda")], 0.0, torch.tensor(1e-44, device="cuda"),
+                            outs=[out])
+    assert (out == 0).all()
+
+
+@pytest.mark.parametrize("max_norm,norm", [(1e-45, 1e-14), (1e-45, 3e38), (1e-40, 1e-9), (2.0 ** -126, 2.0 ** -25), (200.0, 3e38),
+                                           (2.0 ** 27, 2.0 ** 127.99), (2.0 ** -100, 1.0), (2.0 ** -101, 1.0), (1e-38, 1e-7)])
+def test_factors_around_the_two_steps(max_norm, norm):
+    """Where the factor begins to be applied in two steps, and at its ends."""
+    n, m = (float(torch.tensor(v, dtype=FP)) for v in (norm, max_norm))
+    g = rand(500, seed=3, mul=norm / 8).clamp(-norm, norm)
+    out = torch.empty_like(g)
+    ra.ring_attn_grad_scale([g], max_norm, torch.tensor(norm, dtype=FP, device="cuda"), outs=[out])
+    ref.within("scaled", out, ref.f64(g) * (m / n), 4 * 2.0 ** -24 * ref.f64(g).abs() * (m / n) + 2.0 ** -149)
